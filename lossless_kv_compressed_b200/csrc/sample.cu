@@ -175,8 +175,9 @@ __global__ void __launch_bounds__(kStatThreads, kStatBlocks) sample_stat_kernel(
   const int k = a.n_q - 1;
   const int64_t row = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
   const int64_t n_target = (int64_t)a.B * a.n_q;
+  // (rows that fill up the grid's last plane are nobody's, whether or not there are draft rows)
+  if (row >= n_target + (a.draft_logits ? (int64_t)a.B * k : 0)) return;
   const bool draft = row >= n_target;
-  if (draft && row - n_target >= (int64_t)a.B * k) return;
   const int b = (int)(draft ? (row - n_target) / k : row / a.n_q);
   const int i = (int)(draft ? (row - n_target) % k : row % a.n_q);
   const int n = live_drafts(a, b);

@@ -141,3 +141,14 @@ def test_captured_twice_and_replayed_on_two_streams():
     torch.cuda.synchronize()
     for (r, _), w in zip(outs, wants):
         assert torch.equal(r["commit"], w)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,k", [(8200, 3), (16385, 1), (65535, 0), (128, 256)])
+def test_more_rows_than_one_plane_of_the_grid(B, k, dtype):
+    """Row counts above 32768 and no multiple of it, with and without draft logits: the rows that
+    fill up the grid's last plane belong to no sequence."""
+    lg, ql, d, u = make(B, k, 7, B, dtype)
+    check(lg, d, u)
+    if k:
+        check(lg, d, u, ql)
