@@ -291,25 +291,29 @@ constexpr int kTable = 64;
 __device__ __forceinline__ void fill_table(double* table) {
   if (threadIdx.x < kTable) table[threadIdx.x] = exp2(threadIdx.x * (1.0 / kTable));
 }
-// Weights e^((x - m) / T) of a row: with k = 64 / (T ln 2), y = (x - m) k = n + r, |r| <= 1/2,
+// Weights e^((x - m) / T) of a row: with k = 64 / (T ln 2), d = x - m, d k = n + r, |r| <= 1/2,
 //   e^((x - m) / T) = 2^(n / 64) e^(r ln 2 / 64);
-// 0 where y < -64512 (2^-1008), and for x = -inf.
+// 0 where d k < -64512 (2^-1008), and for x = -inf.  The difference is taken first: it is 0 at
+// the largest logit whatever m / T is (m k alone may be large enough for its rounding to pass
+// the ends of the exponent).
 struct Expo {
-  double k, off;             // y = fma(x, k, off)
+  double k, m;
+  double least;              // of d
 };
 __device__ __forceinline__ Expo expo_of(float m, double inv_t) {
   Expo e;
   e.k = 92.33248261689366 * inv_t;                      // 64 / ln 2
-  e.off = -(double)m * e.k;
+  e.m = (double)m;
+  e.least = -64512.0 / e.k;
   return e;
 }
 __device__ __forceinline__ double weight64(double x, Expo e, const double* table) {
-  const double y = fma(x, e.k, e.off);
-  if (!(y > -64512.0)) return 0.0;
+  const double d = x - e.m;
+  if (!(d > e.least)) return 0.0;
   const double shift = 6755399441055744.0;              // 1.5 * 2^52: rounds to an integer
-  const double z = y + shift;
+  const double z = fma(d, e.k, shift);
   const int n = __double2loint(z);
-  const double r = y - (z - shift);
+  const double r = fma(d, e.k, shift - z);
   // (ln 2 / 64)^i / i!
   double p = fma(r, 5.732851688640402e-10, 2.1173137155464774e-07);
   p = fma(r, p, 5.864904955056169e-05);

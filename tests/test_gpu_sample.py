@@ -152,3 +152,20 @@ def test_more_rows_than_one_plane_of_the_grid(B, k, dtype):
     check(lg, d, u)
     if k:
         check(lg, d, u, ql)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,gain", [(1e-18, 60.0), (3e-18, 2000.0), (1e-15, 60.0), (1e-9, 1e4),
+                                    (1.0, 1e19), (1.0, 1e20), (0.3, 1e37)])
+def test_logits_far_larger_than_the_temperature(T, gain, dtype):
+    """Nearly all of p on the largest logit, however large it is against T: it weighs 1."""
+    lg, ql, d, u = make(6, 3, 3001, 11, dtype)
+    lg = (lg.float() * (gain / 10)).to(dtype)
+    ql = (ql.float() * (gain / 10)).to(dtype)
+    lg[2:4, :, 5] = lg[2:4].amax(-1)               # a tie: half of p each
+    d[1:4] = lg[1:4, :3].float().argmax(-1).to(torch.int32)
+    ql[1, torch.arange(3), d[1].long()] = ql[1].amax(-1)
+    t = torch.full((6,), T)
+    w = check(lg, d, u, None, t)
+    assert w["accept_len"][1] == 3 and not w["err"].any()
+    check(lg, d, u, ql, t)
