@@ -623,7 +623,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, PT>::kThreads, 1)
                 tc::tc_fence_after();
               }
               const float alpha = up ? ex2(m_ref - top) : 1.f;
-              if (up) m_ref = top == INFINITY ? NAN : top;     // (inf - inf is NaN in a softmax)
+              // inf - inf is NaN in a softmax.  A NaN stays: a masked tile behind it has a maximum
+              // of -inf, and that as the reference would say that the row has seen nothing.
+              if (up) m_ref = top == INFINITY || m_ref != m_ref ? NAN : top;
               if constexpr (k8) {                      // to the new reference
                 const float by = ref - (m_ref == -INFINITY ? 0.f : m_ref);
 #pragma unroll
