@@ -416,7 +416,8 @@ vc_status vc_paged_read(const vc_paged_cache* cache, int64_t start0, const int32
  * (fp16 for 8-bit rows of small blocks).  Results are the same for every run of the same
  * call, but the way the keys are split, and with it the last bits, depends on the batch.
  * Keys and values of live positions must be finite; those of other slots may hold
- * anything.  A score that passes fp32's range makes its row NaN (+inf), and a row whose
+ * anything.  (A NaN in a live row, the e4m3 code for it included, reaches every row that sees
+ * it; in a value also rows before it in the same call.)  A score that passes fp32's range makes its row NaN (+inf), and a row whose
  * scores are all -inf counts as one that sees no key. */
 size_t vc_paged_attn_workspace_size(const vc_paged_cache* cache, int N, int Hq, int max_q);
 vc_status vc_paged_attn(const vc_paged_cache* cache, const void* q, int64_t q_tok_stride,

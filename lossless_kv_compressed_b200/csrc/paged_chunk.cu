@@ -192,17 +192,25 @@ __device__ __forceinline__ void ex2_poly(uint64_t x, float& a, float& b) {
 }
 
 // ------------------------------------------------------------------ codes to bf16
-// Four codes of a word as bf16 pairs, exactly.
+// codes_to_bf16 takes an e4m3 NaN (0x7f, 0xff) for the 480 that its bits would be; this makes it
+// one again.
+__device__ __forceinline__ void put_nan(uint2& r) {
+  r.x |= __vcmpeq2(r.x & 0x7fff7fffu, 0x43f043f0u) & 0x7fff7fffu;
+  r.y |= __vcmpeq2(r.y & 0x7fff7fffu, 0x43f043f0u) & 0x7fff7fffu;
+}
+// Four codes of a word as bf16 pairs, exactly.  most: the largest e4m3 magnitude bits so far in
+// each half, which are 0x07f0 if one of the codes is a NaN (and the pairs then need put_nan).
 template <int PT>
-__device__ __forceinline__ uint2 codes_to_bf16(uint32_t w) {
-  uint32_t r[2];
+__device__ __forceinline__ uint2 codes_to_bf16(uint32_t w, uint32_t& most) {
+  uint32_t r[2], mag[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if constexpr (PT == VC_PAGE_E4M3) {
       // code s eeee fff as bf16 s 0000eeee fff0000 is 2^-120 of its value (subnormal codes
       // too, as subnormal bf16)
       const uint32_t x = __byte_perm(w, 0, i ? 0x3424 : 0x1404);       // codes in the high bytes
-      const uint32_t y = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+      mag[i] = (x >> 4) & 0x07f007f0u;
+      const uint32_t y = mag[i] | (x & 0x80008000u);
       asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[i]) : "r"(y), "r"(0x7b807b80u));   // 2^120
     } else {
       // 128 + low 7 bits, less 128, or 256 where the sign bit is set
@@ -212,6 +220,7 @@ __device__ __forceinline__ uint2 codes_to_bf16(uint32_t w) {
       asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r[i]) : "r"(a), "r"(b));
     }
   }
+  if constexpr (PT == VC_PAGE_E4M3) most = __vimax3_u16x2(most, mag[0], mag[1]);
   return make_uint2(r[0], r[1]);
 }
 
@@ -797,11 +806,17 @@ __global__ void __launch_bounds__(ChunkCfg<D, PT>::kThreads, 1)
           if (!ok) break;
         }
         uint8_t* at = smem + L::kRing + (2 * st + kv) * L::kTile;
-#pragma unroll
-        for (int y = 0; y < kPer; ++y) {
+        uint32_t most = 0;
+        auto put = [&](int y, uint4 codes, auto nan_tag) {
           const int row = y * kRowsPer + row0;
-          uint2 c0 = codes_to_bf16<PT>(x[y].x), c1 = codes_to_bf16<PT>(x[y].y);
-          uint2 c2 = codes_to_bf16<PT>(x[y].z), c3 = codes_to_bf16<PT>(x[y].w);
+          uint2 c0 = codes_to_bf16<PT>(codes.x, most), c1 = codes_to_bf16<PT>(codes.y, most);
+          uint2 c2 = codes_to_bf16<PT>(codes.z, most), c3 = codes_to_bf16<PT>(codes.w, most);
+          if constexpr (decltype(nan_tag)::value) {
+            put_nan(c0);
+            put_nan(c1);
+            put_nan(c2);
+            put_nan(c3);
+          }
           if (kv == 1 && row >= live) c0 = c1 = c2 = c3 = make_uint2(0u, 0u);
           const uint4 a = make_uint4(c0.x, c0.y, c1.x, c1.y), b = make_uint4(c2.x, c2.y, c3.x, c3.y);
           // pieces 2 piece, 2 piece + 1 of the bf16 row; at D 128 the two halves' lanes write
@@ -811,6 +826,17 @@ __global__ void __launch_bounds__(ChunkCfg<D, PT>::kThreads, 1)
           const uint4 fst = flip ? b : a, snd = flip ? a : b;
           *reinterpret_cast<uint4*>(dst + (((p0 + flip) ^ (row & 7)) << 4)) = fst;
           *reinterpret_cast<uint4*>(dst + (((p0 + 1 - flip) ^ (row & 7)) << 4)) = snd;
+        };
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) put(y, x[y], std::false_type{});
+        // A NaN is put in behind the plain conversion.  Looking for it costs 32 rows over 32K 321 ->
+        // 343 us, 33 rows 359 -> 363, a 2048-token chunk nothing (in the loop itself: 360, 378 and
+        // 1371 -> 1438; from the codes, before the wait: 336, 364 and 1389).
+        if (PT == VC_PAGE_E4M3 && ((most + 0x00100010u) & 0x08000800u)) {
+#pragma unroll 1
+          for (int y = 0; y < kPer; ++y)
+            put(y, *reinterpret_cast<const uint4*>(smem + L::kRawRing + (2 * rs + kv) * L::kRaw +
+                                                   (y * 128 + tid) * 16), std::true_type{});
         }
         tc::fence_proxy_async();
         __syncwarp();
