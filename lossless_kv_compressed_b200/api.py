@@ -394,13 +394,14 @@ def _same_device(dev, **tensors):
             raise ValueError(f"{n}: on {t.device}, expected {dev}")
 
 
-def _on(stream):
+def _on(stream, dev):
     """Context in which a call's own tensors are made: they belong to the stream that uses
-    them, or freeing them here would hand their memory on while that stream still runs."""
+    them, or freeing them here would hand their memory on while that stream still runs.  A
+    stream given as a number is one of ``dev``, whichever device is current."""
     if stream is None:
         return contextlib.nullcontext()
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
     return torch.cuda.stream(stream)
 
 
@@ -593,7 +594,7 @@ def paged_attn(q: torch.Tensor, cache: PagedCache, cu_q: Optional[torch.Tensor] 
     N, Hq, tok, head = _new_rows(q, "q", D, dev)
     cu = _cu(cu_q, cache.B, dev)
     if out is None:
-        with _on(stream):
+        with _on(stream, dev):
             out = (torch.empty if cu_q is None else torch.zeros)((N, Hq, D), dtype=q.dtype, device=dev)
     elif out.shape != q.shape or not out.is_contiguous() or out.device != dev:
         raise ValueError("out: expected a contiguous [N, Hq, D] on the cache's device")
@@ -612,7 +613,7 @@ def paged_attn(q: torch.Tensor, cache: PagedCache, cu_q: Optional[torch.Tensor] 
         if stream is None:
             ws = torch.empty(size, dtype=torch.uint8, device=dev)
         else:
-            with _on(stream):
+            with _on(stream, dev):
                 ws = torch.empty(size, dtype=torch.uint8, device=dev)
     elif ws.device != dev or not ws.is_contiguous():
         raise ValueError("ws: expected a contiguous tensor on the cache's device")
@@ -663,7 +664,7 @@ def accept_sample(logits: torch.Tensor, drafts: Optional[torch.Tensor], u: torch
     if drafts is not None and drafts.numel() == 0:
         drafts = draft_logits = None
     i32 = dict(dtype=torch.int32, device=dev)
-    with _on(stream):
+    with _on(stream, dev):
         if accept_len is None and commit is None and n_commit is None and err_flag is None:
             # one allocation; each is contiguous
             accept_len, n_commit, err_flag, commit = torch.empty((n_q + 3) * B, **i32).split(

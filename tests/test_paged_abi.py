@@ -110,3 +110,23 @@ def test_python_checks():
         vc.accept_sample(torch.zeros((1, 1, 5), dtype=torch.float64), None, torch.zeros((1, 1)))
     with pytest.raises(ValueError):
         vc.accept_sample_workspace_size(0, 1, 5)
+
+
+@pytest.mark.parametrize("handle", [12345, 0])
+def test_a_stream_given_as_a_number_is_one_of_the_calls_device(monkeypatch, handle):
+    """A call's own tensors are made on that stream of the cache's device, not on a stream of the
+    same number of the device that happens to be current."""
+    from lossless_kv_compressed_b200 import api
+    made = []
+
+    class External:
+        def __init__(self, ptr, device=None):
+            self.cuda_stream, self.device = ptr, device
+
+    monkeypatch.setattr(torch.cuda, "ExternalStream", External)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: made.append(s))
+    api._on(handle, torch.device("cuda:1"))
+    assert made[0].cuda_stream == handle and made[0].device == torch.device("cuda:1")
+    own = External(7)
+    api._on(own, torch.device("cuda:1"))
+    assert made[1] is own
