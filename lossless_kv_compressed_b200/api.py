@@ -394,6 +394,15 @@ def _same_device(dev, **tensors):
             raise ValueError(f"{n}: on {t.device}, expected {dev}")
 
 
+_MOST = 2 ** 31 - 1
+
+
+def _fits(name: str, *sizes):
+    """Sizes go to the library as 32-bit numbers (ctypes would take them modulo 2^32)."""
+    if max(sizes) > _MOST:
+        raise ValueError(f"{name}: a size past 2^31 - 1")
+
+
 def _on(stream, dev):
     """Context in which a call's own tensors are made: they belong to the stream that uses
     them, or freeing them here would hand their memory on while that stream still runs.  A
@@ -450,6 +459,7 @@ class PagedCache:
             if t.stride(3) != 1:
                 raise ValueError(f"{n}: the last dimension must be contiguous")
         n_pages, Hkv, page, D = k.shape
+        _fits("k_pages, page_table", *k.shape, *self.page_table.shape)
         _need(self.page_table, torch.int32, "page_table")
         _need(self.kv_len, torch.int32, "kv_len")
         if self.page_table.dim() != 2 or self.kv_len.shape != self.page_table.shape[:1]:
@@ -513,6 +523,7 @@ def _new_rows(t: torch.Tensor, name: str, D: int, dev):
         raise ValueError(f"{name}: the last dimension must be contiguous")
     if t.device != dev:
         raise ValueError(f"{name}: on {t.device}, expected {dev}")
+    _fits(name, shape[0], shape[1])
     return shape[0], shape[1], tok if shape[0] > 1 else 0, head if shape[1] > 1 else 0
 
 
@@ -568,6 +579,7 @@ def paged_read(cache: PagedCache, k_out: torch.Tensor, v_out: torch.Tensor, star
 
 def paged_attn_workspace_size(cache: PagedCache, N: int, Hq: int, max_q: int = 0) -> int:
     """Workspace bytes of paged_attn for N rows; depends on sizes only."""
+    _fits("N, Hq, max_q", N, Hq, max_q)
     if cache._device.index == torch.cuda.current_device():
         n = lib().vc_paged_attn_workspace_size(cache._ref, N, Hq, max_q)
     else:
@@ -605,6 +617,7 @@ def paged_attn(q: torch.Tensor, cache: PagedCache, cu_q: Optional[torch.Tensor] 
     bound = 0 if max_q is None else int(max_q)
     if bound < 0:
         raise ValueError("max_q: negative")
+    bound = min(bound, N)                          # (it goes to the library as 32 bits)
     if ws is None:
         # the size does not depend on the rows: asked for once per head dim and device
         size = _attn_ws.get((D, dev.index))
@@ -624,6 +637,7 @@ def paged_attn(q: torch.Tensor, cache: PagedCache, cu_q: Optional[torch.Tensor] 
 
 # ------------------------------------------------------------------ acceptance by sampling
 def accept_sample_workspace_size(B: int, n_q: int, V: int) -> int:
+    _fits("B, n_q, V", B, n_q, V)
     n = lib().vc_accept_sample_workspace_size(B, n_q, V)
     if n == 0:
         raise ValueError("accept_sample: invalid sizes")
@@ -648,6 +662,7 @@ def accept_sample(logits: torch.Tensor, drafts: Optional[torch.Tensor], u: torch
     if logits.dim() != 3:
         raise ValueError("logits: expected [B, n_q, V]")
     B, n_q, V = logits.shape
+    _fits("logits", B, n_q, V)
     if n_q > 1 and drafts is None:
         raise ValueError("drafts: needed when n_q > 1")
     i32 = torch.int32

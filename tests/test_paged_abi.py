@@ -130,3 +130,17 @@ def test_a_stream_given_as_a_number_is_one_of_the_calls_device(monkeypatch, hand
     own = External(7)
     api._on(own, torch.device("cuda:1"))
     assert made[1] is own
+
+
+def test_sizes_past_32_bits_are_refused_not_wrapped():
+    from lossless_kv_compressed_b200 import api
+    big = 2 ** 32 + 4                                # 4 when taken modulo 2^32
+    for sizes in ((big, 1, 5), (1, big, 5), (1, 1, big), (1, 1, 2 ** 31)):
+        with pytest.raises(ValueError):
+            vc.accept_sample_workspace_size(*sizes)
+    cpu = torch.device("cpu")
+    rows = torch.zeros((1, 1, 64), dtype=torch.bfloat16)
+    assert api._new_rows(rows.expand(2 ** 31 - 1, 2, 64), "k", 64, cpu)[:2] == (2 ** 31 - 1, 2)
+    for shape in ((big, 2, 64), (2, big, 64)):
+        with pytest.raises(ValueError):
+            api._new_rows(rows.expand(shape), "k", 64, cpu)
