@@ -47,29 +47,30 @@ __host__ __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
   return a / b;
 }
 
-// sum_{i < n} floor((a i + b) / m) for n, a, b >= 0, m > 0, by the Euclidean recursion.
+// S(n, m, a, b) = sum_{i < n} floor((a i + b) / m) for n, a, b >= 0, m > 0.  Whole multiples of m
+// in a and b give closed sums.  What is left, a, b < m, counts the lattice points (i, j) with
+// 1 <= j <= (a i + b) / m under a line that rises to h = floor((a (n - 1) + b) / m).  Counted by
+// rows instead, row j has n - ceil((j m - b) / a) of them, so that
+//   S(n, m, a, b) = n h - sum_{j = 1..h} ceil((j m - b) / a) = n h - S(h, a, m, m - b + a - 1),
+// where (a, m) goes the way of Euclid's algorithm: a logarithmic number of steps.
 __host__ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
-  int64_t ans = 0;
+  int64_t sum = 0;
+  bool minus = false;
   while (n > 0) {
-    if (a >= m) {
-      const int64_t q = div64(a, m);
-      ans += n * (n - 1) / 2 * q;
-      a -= q * m;
-    }
-    if (b >= m) {
-      const int64_t q = div64(b, m);
-      ans += n * q;
-      b -= q * m;
-    }
-    const int64_t y = a * n + b;
-    if (y < m) break;
-    n = div64(y, m);
-    b = y - n * m;
-    const int64_t t = m;
-    m = a;
-    a = t;
+    const int64_t qa = div64(a, m), qb = div64(b, m);
+    a -= qa * m;
+    b -= qb * m;
+    const int64_t h = div64(a * (n - 1) + b, m);
+    const int64_t part = n * (n - 1) / 2 * qa + n * (qb + h);
+    sum += minus ? -part : part;
+    minus = !minus;
+    b = m - b + a - 1;
+    n = h;
+    const int64_t step = a;
+    a = m;
+    m = step;
   }
-  return ans;
+  return sum;
 }
 
 // Equal shares of a line of `total` pieces for W workers, W <= total: worker w has
