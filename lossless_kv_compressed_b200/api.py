@@ -523,7 +523,8 @@ def _new_rows(t: torch.Tensor, name: str, D: int, dev):
         raise ValueError(f"{name}: the last dimension must be contiguous")
     if t.device != dev:
         raise ValueError(f"{name}: on {t.device}, expected {dev}")
-    _fits(name, shape[0], shape[1])
+    if shape[0] > _MOST:
+        _fits(name, shape[0])
     return shape[0], shape[1], tok if shape[0] > 1 else 0, head if shape[1] > 1 else 0
 
 
@@ -617,7 +618,8 @@ def paged_attn(q: torch.Tensor, cache: PagedCache, cu_q: Optional[torch.Tensor] 
     bound = 0 if max_q is None else int(max_q)
     if bound < 0:
         raise ValueError("max_q: negative")
-    bound = min(bound, N)                          # (it goes to the library as 32 bits)
+    if bound > N:                                  # (it goes to the library as 32 bits)
+        bound = N
     if ws is None:
         # the size does not depend on the rows: asked for once per head dim and device
         size = _attn_ws.get((D, dev.index))
@@ -662,7 +664,8 @@ def accept_sample(logits: torch.Tensor, drafts: Optional[torch.Tensor], u: torch
     if logits.dim() != 3:
         raise ValueError("logits: expected [B, n_q, V]")
     B, n_q, V = logits.shape
-    _fits("logits", B, n_q, V)
+    if B > _MOST or n_q > _MOST or V > _MOST:
+        _fits("logits", B, n_q, V)
     if n_q > 1 and drafts is None:
         raise ValueError("drafts: needed when n_q > 1")
     i32 = torch.int32

