@@ -322,7 +322,7 @@ vc_status vc_evict_select(const float* score, int rows, int64_t score_cap, int64
  *   type         VC_PAGE_BF16, or 8-bit rows with one fp32 scale per (token, kv head) of K
  *                and of V: VC_PAGE_E4M3 (8-bit float, 4 exponent and 3 fraction bits) or
  *                VC_PAGE_INT8; the row's value is code * scale
- *   B, Hkv, D    sequences, kv heads, head dim in {64, 128}
+ *   B, Hkv, D    sequences, kv heads (65535 each at most), head dim in {64, 128}
  *   page         tokens per page: 16, 32, 64, 128 or 256
  *   n_pages      pages of the pool; max_pages: columns of page_table (n_pages * page and
  *                max_pages * page at most 2^31 - 2^16)
@@ -331,7 +331,7 @@ vc_status vc_evict_select(const float* score, int rows, int64_t score_cap, int64
  *                elements; 16-byte aligned base, each stride a positive multiple of 16 bytes
  *                (a stride whose dimension has one entry is not read)
  *   k_scale, v_scale  fp32 [n_pages, Hkv, page] contiguous, > 0 (8-bit types; else NULL).
- *                Attention takes a value scale under 2^-90 as 2^-90.
+ *                Attention may take a value scale under 2^-90 as 2^-90 (few rows do).
  *   page_table   int32 [B, max_pages]: position t of sequence b is row t % page of page
  *                page_table[b, t / page]; entries past the sequence's last page are not read
  *   kv_len       int32 [B]: tokens of each sequence, the new ones of a call included
@@ -391,9 +391,9 @@ vc_status vc_paged_write(const vc_paged_cache* cache, const void* k, int64_t k_t
 
 /* Read rows back into a contiguous bf16 cache (the layout of vc_verify_attn and of the
  * compressors): row r of k_out, v_out bf16 [B, Hkv, T_cap, D] becomes position start + r
- * of the sequence (8-bit rows: code * scale, rounded once), for 0 <= r < T_cap and
- * 0 <= start + r < kv_len[b]; other rows are left as they were.  start is starts[b]
- * (device int32 [B]) or start0 when starts is NULL. */
+ * of the sequence (8-bit rows: the fp32 product code * scale, rounded to bf16), for
+ * 0 <= r < T_cap and 0 <= start + r < kv_len[b]; other rows are left as they were.  start is
+ * starts[b] (device int32 [B]) or start0 when starts is NULL. */
 vc_status vc_paged_read(const vc_paged_cache* cache, int64_t start0, const int32_t* starts,
                         void* k_out, void* v_out, int64_t T_cap, cudaStream_t stream);
 
@@ -437,7 +437,8 @@ vc_status vc_paged_attn(const vc_paged_cache* cache, const void* q, int64_t q_to
  * draft_logits NULL: q_i is 1 at d_i (drafts of a greedy drafter).  T = 0 (or under 2^-60):
  * p_i is 1 at the first largest logit and q_i at d_i (greedy acceptance).
  *   logits  fp32, or bf16 with flags & VC_LOGITS_BF16, [B, n_q, V]; draft_logits [B, n_q - 1, V]
- *           of the same type or NULL; -inf marks a token that cannot be drawn
+ *           of the same type or NULL; both with a 16-byte aligned base (a part of a batch with
+ *           odd V may not have one: refused); -inf marks a token that cannot be drawn
  *   drafts  int32 [B, n_q - 1] (may be NULL when n_q == 1)
  *   u       fp64 [B, n_q], each in [0, 1): entries 0 .. n_q - 2 decide the drafts, the last
  *           draws x
@@ -448,8 +449,12 @@ vc_status vc_paged_attn(const vc_paged_cache* cache, const void* q, int64_t q_to
  *           negative or not finite (taken as 0), a target row that was looked at (positions
  *           0 .. a) with a NaN, a +inf or nothing above -inf (its draft is refused and x is
  *           vc_accept's argmax of that row), a draft row with the same (q_i is 1 at d_i)
- *   ws      vc_accept_sample_workspace_size(...) bytes; n_q <= 257, V < 2^31 - 2^16
- * The running sums are fp64, so the same inputs give the same tokens.
+ *   ws      vc_accept_sample_workspace_size(...) bytes, 16-byte aligned; B <= 65535, n_q <= 257,
+ *           V < 2^31 - 2^16
+ * The same inputs give the same tokens.  The running sums that x is picked by are fp64; the sums
+ * that turn logits into p_i(d_i) and q_i(d_i) are of fp32 terms, off by some 1e-7 of their value
+ * (under 1e-5 for 128K tokens), so that a draft with u q_i(d_i) that near to p_i(d_i) may be
+ * decided the other way.
  * ---------------------------------------------------------------------------- */
 #define VC_LOGITS_BF16 8
 size_t vc_accept_sample_workspace_size(int B, int n_q, int V);

@@ -656,7 +656,8 @@ def accept_sample(logits: torch.Tensor, drafts: Optional[torch.Tensor], u: torch
     [B, n_q - 1] int32 and random numbers u [B, n_q] fp64 in [0, 1): the committed tokens are
     samples of softmax(logits / temperature).  draft_logits [B, n_q - 1, V] (the logits' type):
     what the drafts were drawn from; without it they count as drawn with probability one.
-    temperature fp32 [B] (0: greedy), n_drafts int32 [B] (a sequence's live drafts)."""
+    temperature fp32 [B] (0: greedy), n_drafts int32 [B] (a sequence's live drafts).  logits and
+    draft_logits start on 16-byte boundaries."""
     dtype, dev = logits.dtype, logits.device
     if dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"logits: expected float32 or bfloat16, got {dtype}")
