@@ -324,6 +324,13 @@ __device__ __forceinline__ double weight64(double x, Expo e, const double* table
   return __hiloint2double(__double2hiint(w) + ((n >> 6) << 20), __double2loint(w));
 }
 
+// max(p - q, 0) from the weights of both rows and one over their sums.  Both products are rounded
+// (fused, one of them would be exact and p - p its rounding), so that it is 0 where p == q, and
+// the pick meets the very numbers that were summed.
+__device__ __forceinline__ double residual_of(double e_p, double w_p, double e_q, double w_q) {
+  return fmax(__dsub_rn(__dmul_rn(e_p, w_p), __dmul_rn(e_q, w_q)), 0.0);
+}
+
 // Sum over the block, in the same order every time; sh: kPassWarps values.
 __device__ __forceinline__ double block_sum(double s, double* sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -581,7 +588,7 @@ __device__ __forceinline__ void residual_part(const SampleArgs& a, int b, int bl
     double r[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
     for (int i = 0; i < kSeg / 32; ++i)
-      r[i & 3] += fmax(weight64(vp.v[i], ep, table) * wp - weight64(vq.v[i], eq, table) * wq, 0.0);
+      r[i & 3] += residual_of(weight64(vp.v[i], ep, table), wp, weight64(vq.v[i], eq, table), wq);
     const double s = warp_sum((r[0] + r[1]) + (r[2] + r[3]));
     if (lane == 0) a.sums[(2 * (int64_t)a.B + b) * a.n_seg + seg] = s;
   }
@@ -689,7 +696,7 @@ __device__ __forceinline__ void pick_part(const SampleArgs& a, int b, const doub
         if (j < a.V && j != skip) {
           wj[x] = weight64(to_f32(xp[j]), ep, table);
           if (mode == kResidual)
-            wj[x] = fmax(wj[x] * wp - weight64(to_f32(xq[j]), eq, table) * wq, 0.0);
+            wj[x] = residual_of(wj[x], wp, weight64(to_f32(xq[j]), eq, table), wq);
         }
         sum += wj[x];
       }

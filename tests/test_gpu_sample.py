@@ -169,3 +169,22 @@ def test_logits_far_larger_than_the_temperature(T, gain, dtype):
     w = check(lg, d, u, None, t)
     assert w["accept_len"][1] == 3 and not w["err"].any()
     check(lg, d, u, ql, t)
+
+
+@pytest.mark.parametrize("V", [700, 40000])
+@pytest.mark.parametrize("shift", [0.0, 1.0])
+def test_equal_rows_refused_at_the_last_number(V, shift):
+    """p == q to the last bit and u one step below 1: whether u q < p then depends on rounding.
+    Where a draft is refused, max(p - q, 0) is 0 everywhere and the token comes from p."""
+    B, k = 60, 3
+    lg, _, _, u = make(B, k, V, V)
+    lg = (lg * 1024).round() / 1024                # adding 1 is exact
+    ql = (lg[:, :k] + shift).contiguous()
+    d = torch.distributions.Categorical(logits=ql).sample().to(torch.int32)
+    u[:, :k] = 1.0 - 2.0 ** -53
+    r = vc.accept_sample(lg.cuda(), d.cuda(), u.cuda(), ql.cuda())
+    a, commit = r["accept_len"].cpu().numpy(), r["commit"].cpu().numpy()
+    assert not r["err"].any() and (a < k).any()
+    for b in range(B):
+        c = np.cumsum(sample.probabilities(lg[b, a[b]].double().numpy(), 1.0))
+        assert commit[b, a[b]] == np.nonzero(c > u[b, k].item() * c[-1])[0][0], b
