@@ -438,7 +438,8 @@ vc_status vc_paged_attn(const vc_paged_cache* cache, const void* q, int64_t q_to
  * p_i is 1 at the first largest logit and q_i at d_i (greedy acceptance).
  *   logits  fp32, or bf16 with flags & VC_LOGITS_BF16, [B, n_q, V]; draft_logits [B, n_q - 1, V]
  *           of the same type or NULL; both with a 16-byte aligned base (a part of a batch with
- *           odd V may not have one: refused); -inf marks a token that cannot be drawn
+ *           odd V may not have one: refused); -inf marks a token that cannot be drawn, and a
+ *           logit further below its row's largest than fp32's range may count as one
  *   drafts  int32 [B, n_q - 1] (may be NULL when n_q == 1)
  *   u       fp64 [B, n_q], each in [0, 1): entries 0 .. n_q - 2 decide the drafts, the last
  *           draws x

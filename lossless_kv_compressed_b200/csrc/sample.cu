@@ -114,7 +114,8 @@ __device__ __forceinline__ uint64_t pair(float a, float b) {
 }
 
 // The exponent's factor log2(e) / T in two parts, both > 0: a part of a -inf logit is then -inf
-// whatever the other is, and so is one that overflows.
+// whatever the other is, and so is one that overflows.  (At least the smallest fp32 number: next
+// to a factor of 1e-38, for T near the largest, more would count.)
 struct Factor {
   float hi, lo;
 };
@@ -122,7 +123,7 @@ __device__ __forceinline__ Factor factor_of(float t) {
   const double c = 1.4426950408889634 / (double)t;
   Factor f;
   f.hi = __double2float_rz(c);
-  f.lo = fmaxf((float)(c - (double)f.hi), 1e-37f);
+  f.lo = fmaxf((float)(c - (double)f.hi), 1.4e-45f);
   return f;
 }
 // 2^(d (hi + lo)) for d <= 0.

@@ -188,3 +188,14 @@ def test_equal_rows_refused_at_the_last_number(V, shift):
     for b in range(B):
         c = np.cumsum(sample.probabilities(lg[b, a[b]].double().numpy(), 1.0))
         assert commit[b, a[b]] == np.nonzero(c > u[b, k].item() * c[-1])[0][0], b
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,gain", [(1e30, 1e30), (1e36, 1e36), (1e38, 2e37), (1e38, 4e37), (3.3e38, 4e37)])
+def test_temperatures_up_to_the_largest(T, gain, dtype):
+    """log2(e) / T near fp32's smallest numbers, logits as large as T: the weights still count."""
+    lg, ql, d, u = make(40, 4, 300, 13, dtype, spread=1.0)
+    lg, ql = ((x.float().clamp(-4, 4) * gain).to(dtype) for x in (lg, ql))
+    lg[::3, :, ::7] = -float("inf")
+    check(lg, d, u, ql, torch.full((40,), T))
+    check(lg, d, u * 2.0 ** -5, None, torch.full((40,), T))
