@@ -417,8 +417,10 @@ vc_status vc_paged_read(const vc_paged_cache* cache, int64_t start0, const int32
  * call, but the way the keys are split, and with it the last bits, depends on the batch.
  * Keys and values of live positions must be finite; those of other slots may hold
  * anything.  (A NaN in a live row, the e4m3 code for it included, reaches every row that sees
- * it; in a value also rows before it in the same call.)  A score that passes fp32's range makes its row NaN (+inf), and a row whose
- * scores are all -inf counts as one that sees no key. */
+ * it; in a value also rows before it in the same call.)  A score that passes fp32's range,
+ * before or after scale, makes its row NaN (+inf), and a row whose scores are all -inf counts as
+ * one that sees no key.  Values are summed in fp32 at up to 2^8 times their weight before the
+ * division, so |v| times the number of keys has to stay under 2^120. */
 size_t vc_paged_attn_workspace_size(const vc_paged_cache* cache, int N, int Hq, int max_q);
 vc_status vc_paged_attn(const vc_paged_cache* cache, const void* q, int64_t q_tok_stride,
                         int64_t q_head_stride, int N, int Hq, const int32_t* cu_q, int max_q,
